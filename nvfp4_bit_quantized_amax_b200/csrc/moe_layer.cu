@@ -41,6 +41,11 @@ __device__ __forceinline__ void store_remote_f64(const void* local, uint32_t cta
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(v) : "memory");
 }
 
+// The cluster's barrier for warps whose lanes may be apart (a loop or a store that not all
+// lanes took comes before): without .aligned each thread arrives for itself.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // A cluster takes TC tokens.  Logits: a warp takes an expert and the cluster's tokens;
 // products of eight elements are added in fp32, those sums in fp64, so that the choice
 // does not hang on the order of the additions or on the batch.  The logits of token r go
@@ -57,7 +62,7 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
     const int rank = blockIdx.x % kRouteCluster, t0 = blockIdx.x / kRouteCluster * TC;
     const int nt = p.T - t0 < TC ? p.T - t0 : TC;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA runs
+    cluster_arrive();  // this CTA runs
     grid_dependents();
     if (threadIdx.x == 0) amax = 0;
     for (int i = blockIdx.x * kRouteThreads + threadIdx.x; i < p.T * p.topk; i += gridDim.x * kRouteThreads)
@@ -92,15 +97,16 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xFFFFFFFFu, acc[t], o);
         if (!joined) {
-            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            cluster_wait();
             joined = true;
         }
 #pragma unroll
         for (int t = 0; t < TC; ++t)
             if (t < nt && lane == t) store_remote_f64(logit + e, (uint32_t)t, acc[t]);
     }
-    if (!joined) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (!joined) cluster_wait();
+    cluster_arrive();
+    cluster_wait();
     if (rank >= nt) return;
     const int t = t0 + rank;
     uint32_t big = 0;  // the row's largest |x|, as integers: their order, NaN largest

@@ -459,9 +459,9 @@ int nvfp4_adamw(const nvfp4_adamw_tensor* tensors, int count, const nvfp4_adamw_
  *   ws   nvfp4_moe_layer_workspace_bytes() bytes, 256-byte aligned; scratch of one call
  *        (no status word); calls that overlap on the GPU need one each.
  *   tokens 1 .. 128, E 1 .. 1024, topk 1 .. min(E, 16), K and F multiples of 128 up to
- *   16384.  The projections' intermediate rows are held to 11 significant bits relative
- *   to their largest element; every sum is fp32 or wider, in an order that depends on
- *   the sizes and the routing alone.
+ *   16384.  The rows between the projections are held to 22 significant bits, or to 2^-50
+ *   of their largest element; every sum is fp32 or wider, in an order that depends on the
+ *   sizes and the routing alone.
  */
 enum { NVFP4_SCORE_SOFTMAX = 0, NVFP4_SCORE_SIGMOID = 1 };
 typedef struct nvfp4_moe_layer_opts {

@@ -10,9 +10,13 @@
 // A code times its block scale has at most 6 significant bits and lies in 2^-10 ..
 // 2688: exact in fp16, which the hardware decodes two codes at a time.  The activations
 // are held in fp16 too, each row scaled by a power of two to a maximum in [2^14, 2^15):
-// bf16 rows then lose nothing above 2^-32 of their maximum, and the fp32 rows between
-// the projections keep 11 bits.  The products go through mma.m16n8k16 with 16 weight
-// rows as M and 8 tokens as N, accumulated in fp32.
+// bf16 rows then lose nothing above 2^-32 of their maximum.  The fp32 rows between the
+// projections are split, v = hi + 2^-11 lo with hi = fp16(v) and lo = fp16(2^11 (v - hi)):
+// 2^-22 of a value, or 2^-50 of its row's maximum, is all that is lost (hi alone: 2^-11,
+// which showed in y as a relative difference of 9e-4).  The products go through mma.m16n8k16
+// with 16 weight rows as M and 8 columns as N, accumulated in fp32; a column is a token, in
+// the second projection one of a token's two parts, side by side, so that one thread holds
+// both sums.
 //
 // Measured (a captured call, weights from memory): 64 experts of 2048 x 1024, top 4: 22 us
 // for 1 token, 55 us for 16 (146 MB of weights: 22 us at 6.5 TB/s); 128 experts of 4096 x
@@ -200,9 +204,9 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 // decoded into tensor memory for tcgen05 fp16 MMAs: 536 (130 cycles for each M = 128, N =
 // 16 MMA).  All warps on one tile, for contiguous reads: above 560 (a join per tile).
 constexpr int kExpWarps = 16, kExpThreads = kExpWarps * 32;
-constexpr int kMaxTiles = 4;            // 8-token tiles of one pass
+constexpr int kMaxTiles = 4;            // 8-column tiles of one pass
 // Share of the work.  With a dozen items or more a CTA, where experts have unlike numbers of
-// tokens, an item counts as its passes over the weights plus its 8-token tiles; with fewer,
+// tokens, an item counts as its passes over the weights plus its 8-column tiles; with fewer,
 // what counts is how many tiles a CTA's warps have to split at a time, and every item counts
 // alike.  Measured, alike and counted (us): 64 tokens, 128 experts of 4096 x 2048, top 8
 // (110 items a CTA) 539 and 390; 128 tokens, 64 of 1024 x 1024, top 8 (14 to 28) 96 and 83;
@@ -217,7 +221,8 @@ constexpr int kStageBytes = 4 * 512 + kScaleBytes;  // of one warp: 32 rows x 64
 // Shared memory of a launch: byte offsets after the rings (which start at 0).
 struct ExpPlan {
     int depth;       // stages of a warp's ring
-    int cap, cols;   // tokens of a pass; columns of a token tile (8, or cap if that is less)
+    int cap, cols;   // tokens of a pass; columns of a tile (8, or those of cap tokens if that is less)
+    int tiles;       // the most tiles of a pass
     int x, red, lists, bytes;
 };
 
@@ -276,7 +281,7 @@ __device__ __forceinline__ void copy_wait() {
 // elements 4 j .. 4 j + 3 of each of the four lanes t.
 //   code: this lane's 16 bytes of row (tile, half) (2 tile + half) * 512 on; sc: its two
 //   scales, 32 bytes on per row.  xb: the tokens' 16-byte units of this lane, `xstep`
-//   apart for consecutive eights of columns, `xtile` for token tiles.
+//   apart for consecutive eights of the reduction, `xtile` for tiles of columns.
 struct StageRegs {
     uint4 w[2][2];
     uint32_t s[2][2];
@@ -350,11 +355,17 @@ struct Cursor {
     bool on, end;
 };
 
-// MT: the most token tiles of a pass (registers for their sums).
+// Columns of the MMA that a token takes, and what its second one (v - hi) is scaled by.
+template <bool DOWN>
+constexpr int kParts = DOWN ? 2 : 1;
+constexpr float kLowUp = 2048.0f, kLowDown = 1.0f / 2048.0f;
+
+// MT: the most tiles of columns of a pass (registers for their sums).
 template <bool DOWN, int MT>
 __global__ void __launch_bounds__(kExpThreads, 1) moe_expert_kernel(const MoeLayerParams p, const ExpPlan pl) {
     extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ float row_scale[8 * MT];
+    constexpr int P = kParts<DOWN>;
+    __shared__ float row_scale[8 * MT / P];
     __shared__ int nactive, even;
     const int nslots = p.T * p.topk;
     uint32_t* const count = reinterpret_cast<uint32_t*>(sm + pl.lists);  // tokens of each expert
@@ -407,14 +418,14 @@ __global__ void __launch_bounds__(kExpThreads, 1) moe_expert_kernel(const MoeLay
         }
         // Experts with more tokens than a tile or a pass holds cost more per weight tile.
         most = __reduce_max_sync(0xFFFFFFFFu, most);
-        const bool uneven = (int)most > pl.cols && nact * tiles >= kCountedItems * (int)gridDim.x;
+        const bool uneven = (int)most * P > pl.cols && nact * tiles >= kCountedItems * (int)gridDim.x;
         if (uneven) {
             int load = 0;
             __syncwarp();
             for (int a0 = 0; a0 < nact; a0 += 32) {
                 const int a = a0 + lane, c = a < nact ? (int)count[active[a]] : 0;
                 const int passes = (c + pl.cap - 1) / pl.cap;
-                const int own = c > 0 ? passes + max(passes, (c + 7) / 8) : 0;
+                const int own = c > 0 ? passes + max(passes, (c * P + 7) / 8) : 0;
                 int s = own;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -534,7 +545,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) moe_expert_kernel(const MoeLay
     float* const red = reinterpret_cast<float*>(sm + pl.red);
     const uint32_t xs = smem_addr(sm + pl.x);
     const uint32_t xstep = (uint32_t)pl.cols * 64u, xtile = (uint32_t)steps * 4u * xstep;
-    // (columns past a tile's tokens repeat its first; their sums are not used)
+    // (columns past a tile's repeat its first; their sums are not used)
     const uint32_t xlane = xs + (g < pl.cols ? (uint32_t)g * 64u : 0u) + (uint32_t)t * 16u;
     const uint32_t sc_off = 4 * 512 + (uint32_t)(t >> 1) * 160u + (uint32_t)g * 4u + (uint32_t)(t & 1) * 2u;
     uint32_t stage = ring;
@@ -543,18 +554,19 @@ __global__ void __launch_bounds__(kExpThreads, 1) moe_expert_kernel(const MoeLay
     while (!cp.end) {
         const int n_e = (int)count[cp.e];
         const int np = n_e - cp.p0 < pl.cap ? n_e - cp.p0 : pl.cap;
-        const int nt = (np + 7) / 8;
+        const int nt = (np * P + 7) / 8;
         const uint16_t* const my_slots = slots + start[cp.e] + cp.p0;
         if (fresh) {
             // ---- the tokens' rows as scaled fp16 in fragment order: 16-byte unit
-            // (token, k / 8) at [tile][k / 128][(k % 32) / 8][token][(k % 128) / 32]
+            // (column, k / 8) at [tile][k / 128][(k % 32) / 8][column][(k % 128) / 32]
             __syncthreads();  // the slots are in place; the previous pass has read its rows
-            const int rows_pad = pl.cols < 8 ? pl.cols : nt * 8;
+            const int rows_pad = (pl.cols < 8 ? pl.cols : nt * 8) / P;
             for (int u = threadIdx.x; u < rows_pad * steps * 16; u += kExpThreads) {
                 const int i = u / (steps * 16), w = u - i * (steps * 16), k = w * 8;
-                const uint32_t dst = xs + (uint32_t)(i >> 3) * xtile + (uint32_t)((w >> 4) * 4 + (w & 3)) * xstep +
-                                     (uint32_t)(i & 7) * 64u + (uint32_t)((w >> 2) & 3) * 16u;
-                uint32_t o[4] = {0, 0, 0, 0};
+                const int col = i * P;
+                const uint32_t dst = xs + (uint32_t)(col >> 3) * xtile + (uint32_t)((w >> 4) * 4 + (w & 3)) * xstep +
+                                     (uint32_t)(col & 7) * 64u + (uint32_t)((w >> 2) & 3) * 16u;
+                uint32_t o[4] = {0, 0, 0, 0}, low[4] = {0, 0, 0, 0};
                 if (i < np) {
                     const int slot = my_slots[i];
                     float down, up;
@@ -574,12 +586,25 @@ __global__ void __launch_bounds__(kExpThreads, 1) moe_expert_kernel(const MoeLay
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const __half2 h = __floats2half2_rn(v[2 * q] * down, v[2 * q + 1] * down);
+                        const float a = v[2 * q] * down, b = v[2 * q + 1] * down;  // exact: |a|, |b| < 2^15
+                        const __half2 h = __floats2half2_rn(a, b);
                         o[q] = *reinterpret_cast<const uint32_t*>(&h);
+                        if (DOWN) {
+                            const float2 f = __half22float2(h);
+                            float da = a - f.x, db = b - f.y;  // infinities stay in the first part alone
+                            da = da == da ? da : 0.0f;
+                            db = db == db ? db : 0.0f;
+                            const __half2 l = __floats2half2_rn(da * kLowUp, db * kLowUp);
+                            low[q] = *reinterpret_cast<const uint32_t*>(&l);
+                        }
                     }
                 }
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                              : "memory");
+                if (DOWN)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 64u), "r"(low[0]), "r"(low[1]),
+                                 "r"(low[2]), "r"(low[3])
+                                 : "memory");
             }
             __syncthreads();
         }
@@ -648,15 +673,17 @@ __global__ void __launch_bounds__(kExpThreads, 1) moe_expert_kernel(const MoeLay
             for (int n = 0; n < MT; ++n) {
                 if (n >= nt) break;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int m = n * 8 + 2 * t + c;
+                for (int c = 0; c < 2 / P; ++c) {
+                    const int m = (n * 8 + 2 * t) / P + c;
                     const bool in = m < np;
                     const float scale = in ? row_scale[m] : 0.0f;
                     const int slot = in ? my_slots[m] : 0;
                     uint32_t big = 0;  // the row's largest |h| of this lane
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float v0 = acc[i][n][c] * scale * g_e, v1 = acc[i][n][2 + c] * scale * g_e;
+                        const float s0 = DOWN ? fmaf(acc[i][n][1], kLowDown, acc[i][n][0]) : acc[i][n][c];
+                        const float s1 = DOWN ? fmaf(acc[i][n][3], kLowDown, acc[i][n][2]) : acc[i][n][2 + c];
+                        const float v0 = s0 * scale * g_e, v1 = s1 * scale * g_e;
                         const int r0 = row + i * tile_rows;
                         if (DOWN) {
                             if (in) {
@@ -718,29 +745,32 @@ __global__ void __launch_bounds__(256) moe_sum_kernel(const MoeLayerParams p) {
 
 // ---------------------------------------------------------------- host side
 // Shared memory of a launch.  A pass takes as many tokens as an expert is likely to have
-// (its mean and two standard deviations), in tiles of 8, while the rings keep 3 stages;
-// very long rows leave room for fewer than 8 tokens.
+// (its mean and two standard deviations), in tiles of 8 columns, while the rings keep 3
+// stages; very long rows leave room for fewer than 8 columns.
 static bool plan_expert(const MoeLayerParams& p, bool down, int smem_max, ExpPlan* pl) {
+    const int parts = down ? kParts<true> : kParts<false>;
     const int row_bytes = 2 * (down ? p.F : p.K);
     const int lists = (4 * p.E + 2 * 2 * p.E + 2 * 2 * p.T * p.topk + 2 * (p.E + 1) + 15) / 16 * 16;
     const int room = smem_max - lists;
     const double mean = (double)p.T * p.topk / p.E;
     int likely = (int)(mean + 2.0 * sqrt(mean)) + 1;
     likely = likely > p.T ? p.T : likely;
-    int nt = (likely + 7) / 8;
+    int nt = (likely * parts + 7) / 8;
     nt = nt > kMaxTiles ? kMaxTiles : nt;
-    auto depth = [&](int tokens, int tiles) {
-        const int n = (room - tokens * row_bytes - tiles * kExpWarps * 1024) / (kExpWarps * kStageBytes);
+    auto depth = [&](int columns, int tiles) {
+        const int n = (room - columns * row_bytes - tiles * kExpWarps * 1024) / (kExpWarps * kStageBytes);
         return n > kMaxDepth ? kMaxDepth : n;
     };
     while (nt > 1 && depth(nt * 8, nt) < 3) --nt;
-    pl->cap = nt * 8;
+    int columns = nt * 8;
     pl->cols = 8;
-    while (pl->cap > 1 && depth(pl->cap, nt) < 2) pl->cols = pl->cap = pl->cap / 2;
-    pl->depth = depth(pl->cap, nt);
+    while (columns > parts && depth(columns, nt) < 2) pl->cols = columns = columns / 2;
+    pl->cap = columns / parts;
+    pl->tiles = nt;
+    pl->depth = depth(columns, nt);
     if (pl->depth < 2) return false;
     pl->x = kExpWarps * pl->depth * kStageBytes;
-    pl->red = pl->x + pl->cap * row_bytes;
+    pl->red = pl->x + columns * row_bytes;
     pl->lists = pl->red + nt * kExpWarps * 1024;
     pl->bytes = pl->lists + lists;
     return true;
@@ -786,8 +816,8 @@ static cudaError_t launch_expert(const MoeLayerParams& p, int sms, cudaStream_t 
     const int room = most[dev] - 1024;  // beside the static arrays
     ExpPlan pl;
     if (!plan_expert(p, DOWN, room, &pl)) return cudaErrorInvalidValue;
-    if (pl.cap <= 8) return launch_expert_mt<DOWN, 1>(p, pl, dev, room, sms, st);
-    if (pl.cap <= 16) return launch_expert_mt<DOWN, 2>(p, pl, dev, room, sms, st);
+    if (pl.tiles == 1) return launch_expert_mt<DOWN, 1>(p, pl, dev, room, sms, st);
+    if (pl.tiles == 2) return launch_expert_mt<DOWN, 2>(p, pl, dev, room, sms, st);
     return launch_expert_mt<DOWN, 4>(p, pl, dev, room, sms, st);
 }
 

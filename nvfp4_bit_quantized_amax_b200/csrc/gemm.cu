@@ -316,6 +316,7 @@ __device__ __forceinline__ void epilogue_tile(uint32_t lane_base, int64_t row0, 
             continue;
         }
         uint32_t r[32];
+        __syncwarp();  // as the fp32 stores of the columns before may have parted the lanes
         tmem_ld_32cols(lane_base + (uint32_t)(c * 32), r);
         tmem_wait_ld(r);
         float v[32];
@@ -533,6 +534,7 @@ __device__ __forceinline__ void epilogue_fused(uint32_t lane_base, int64_t row0,
 #pragma unroll 1
         for (int c = 0; c < CW / 32; ++c) {
             uint32_t r[32];
+            __syncwarp();  // the rows' stores may have parted the lanes; the load wants them together
             tmem_ld_32cols(lane_base + (uint32_t)(c * 32), r);
             tmem_wait_ld(r);
 #pragma unroll
@@ -872,8 +874,9 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// Not .aligned: code that one thread of a warp takes comes directly before.
 __device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // Arrive on the peer's barrier without a cluster-scope release: used after
 // tcgen05.wait::st, which has already completed the TMEM writes it announces.

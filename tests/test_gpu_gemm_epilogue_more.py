@@ -1,0 +1,44 @@
+"""GPU tests of the fused GEMM epilogue over many tiles per CTA, where a warp's staging buffer
+passes from one residual box, and one tile, to the next."""
+import pytest
+import torch
+
+from ffn_ref import U
+from gpu_util import DEV
+from nvfp4_bit_quantized_amax_b200 import capi
+
+pytestmark = pytest.mark.gpu
+
+
+def problem(M, N, K, seed):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+
+    def operand(rows):
+        return (torch.randint(0, 256, (rows, K // 2), generator=gen, device=DEV, dtype=torch.uint8),
+                torch.randint(0x20, 0x48, (capi.scale_bytes(rows, K),), generator=gen, device=DEV, dtype=torch.uint8))
+    (A, sA), (B, sB) = operand(M), operand(N)
+    kw = dict(A=A, sfA=sA, B=B, sfB=sB, alpha=0.01 / K ** 0.5, M=M, N=N, K=K)
+    bias = torch.randn(N, generator=gen, device=DEV)
+    res = torch.randn(M, N, generator=gen, device=DEV).bfloat16()
+    return kw, bias, res
+
+
+@pytest.mark.parametrize("M,N,K", [(128, 512, 64), (77, 1000, 320), (33, 264, 64), (1, 8, 64), (100, 340984, 64),
+                                   (300, 1032, 64), (2000, 10248, 128)])
+def test_fp32_output_of_ragged_rows(M, N, K):
+    """fp32 stores that only the rows inside D take, between two loads of the accumulator: the
+    output alone, through both epilogues, equals the one stored beside bf16."""
+    kw, bias, _ = problem(M, N, K, M + N)
+    acc, d, d2 = (torch.full((M, N), float("nan"), device=DEV) for _ in range(3))
+    d16 = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    plain = (kw["A"], kw["sfA"], kw["B"], kw["sfB"], kw["alpha"], M, N, K)
+    capi.nvfp4_gemm(*plain, D_f32=acc, status=status)
+    capi.nvfp4_gemm(*plain, D_f32=d2, D_bf16=d16, status=status)
+    assert torch.equal(acc, d2) and torch.equal(acc.bfloat16(), d16) and acc.isfinite().all()
+    capi.nvfp4_gemm_epilogue(**kw, D_f32=d, act=capi.ACT_RELU2, status=status)
+    ref = acc.double().clamp(min=0).square()  # acc rounded once, the square once
+    assert ((d.double() - ref).abs() <= 3.01 * U * ref + 1e-37).all() and status.item() == 0
+    capi.nvfp4_gemm_epilogue(**kw, D_f32=d, bias=bias, act=capi.ACT_GELU, status=status)
+    capi.nvfp4_gemm_epilogue(**kw, D_f32=d2, D_bf16=d16, bias=bias, act=capi.ACT_GELU, status=status)
+    assert torch.equal(d, d2) and torch.equal(d.bfloat16(), d16) and status.item() == 0

@@ -385,10 +385,12 @@ struct EpiCtx {
     uint32_t buf, bar, phase;
     const CUtensorMap *tmD, *tmZ, *tmR;
 };
-// Start the copy of a residual box into the staging buffer, once the previous store has
-// read it.
+// Start the copy of a residual box into the staging buffer, once every lane has read the
+// box before it (without a bf16 output no store's barrier comes between) and the previous
+// store has.  Called by whole warps.
 template <int CH>
 __device__ __forceinline__ void residual_fetch(const EpiCtx& x, int64_t col, int64_t row0) {
+    __syncwarp();
     if ((threadIdx.x & 31) == 0) {
         bulk_wait_read_all();
         mbar_expect_tx(x.bar, CH * 2u * 32u);

@@ -42,3 +42,32 @@ def test_fp32_output_of_ragged_rows(M, N, K):
     capi.nvfp4_gemm_epilogue(**kw, D_f32=d, bias=bias, act=capi.ACT_GELU, status=status)
     capi.nvfp4_gemm_epilogue(**kw, D_f32=d2, D_bf16=d16, bias=bias, act=capi.ACT_GELU, status=status)
     assert torch.equal(d, d2) and torch.equal(d.bfloat16(), d16) and status.item() == 0
+
+
+# the first two: pairs of CTAs, with 8 tiles each and with ragged rows and columns; the last
+# two: single CTAs (at most 128 rows), 9 tiles each
+MANY_TILES = [(2048, 20480, 64), (2000, 10248, 128), (128, 340992, 64), (77, 340984, 64)]
+
+
+@pytest.mark.parametrize("M,N,K", MANY_TILES)
+def test_residual_with_fp32_output_alone(M, N, K):
+    """D_f32 with a residual and without Z, the one form with no store between two residual
+    boxes: without an activation D is nvfp4_gemm's fp32 output plus the residual."""
+    kw, bias, res = problem(M, N, K, M)
+    acc = torch.full((M, N), float("nan"), device=DEV)
+    capi.nvfp4_gemm(kw["A"], kw["sfA"], kw["B"], kw["sfB"], kw["alpha"], M, N, K, D_f32=acc)
+    d = torch.full((M, N), float("nan"), device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for _ in range(3):
+        d.fill_(float("nan"))
+        capi.nvfp4_gemm_epilogue(**kw, D_f32=d, residual=res, status=status)
+        assert status.item() == 0
+        ref = acc.double() + res.double()
+        # acc is off by half a step of its own, D by half a step of its
+        assert ((d.double() - ref).abs() <= 1.01 * U * (acc.double().abs() + ref.abs())).all()
+    del acc, ref
+    # with the rest of the epilogue, the bf16 output beside it goes through other copies
+    d2, d16 = torch.full_like(d, float("nan")), torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    capi.nvfp4_gemm_epilogue(**kw, D_f32=d, bias=bias, act=capi.ACT_SILU, residual=res)
+    capi.nvfp4_gemm_epilogue(**kw, D_f32=d2, D_bf16=d16, bias=bias, act=capi.ACT_SILU, residual=res)
+    assert torch.equal(d, d2) and torch.equal(d.bfloat16(), d16)

@@ -102,7 +102,8 @@ __global__ void __cluster_dims__(kBwdCluster, 1, 1) __launch_bounds__(256) epilo
         for (int q = 0; q < kBwdCluster; ++q) t += part[q][threadIdx.x];
         sums[cluster * N + c] = t;
     }
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    // (not .aligned: where N % 32 is not 0 the store above has parted the lanes)
+    asm volatile("barrier.cluster.wait;" ::: "memory");
 }
 
 // dbias[n] = sum of the partial rows, in row order by eight threads of a column.

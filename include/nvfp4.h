@@ -364,6 +364,12 @@ int nvfp4_gemm_epilogue(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, 
                         const float* scale_a, const float* scale_b, float alpha, int64_t M, int64_t N,
                         int64_t K, const nvfp4_epilogue* epi, void* D_bf16, float* D_f32, int* status,
                         nvfp4_stream_t stream);
+/* The same with the pipeline waits' bound set by the caller, the residual's among them
+ * (nvfp4_gemm_wait_limit's testing hook): after a timeout D and Z are incomplete. */
+int nvfp4_gemm_epilogue_wait_limit(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
+                                   const float* scale_a, const float* scale_b, float alpha, int64_t M,
+                                   int64_t N, int64_t K, const nvfp4_epilogue* epi, void* D_bf16,
+                                   float* D_f32, int* status, long long wait_cycles, nvfp4_stream_t stream);
 /* nvfp4_linear_fprop_ex whose GEMM applies the epilogue (epi as above; NULL: none):
  * Y = act(X W^T + bias) + residual.  dgrad and wgrad then take the dZ that
  * nvfp4_epilogue_backward makes of dY. */

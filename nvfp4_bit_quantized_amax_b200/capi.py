@@ -36,8 +36,8 @@ EXPORTS = (
     "nvfp4_moe_grouped_workspace_bytes", "nvfp4_moe_grouped_operand", "nvfp4_moe_grouped_fprop",
     "nvfp4_moe_grouped_dgrad", "nvfp4_moe_grouped_wgrad", "nvfp4_gemm_wait_limit",
     "nvfp4_moe_grouped_fprop_gather",
-    "nvfp4_gemm_epilogue", "nvfp4_linear_fprop_epilogue", "nvfp4_epilogue_backward_workspace_bytes",
-    "nvfp4_epilogue_backward", "nvfp4_adamw", "nvfp4_moe_layer_workspace_bytes", "nvfp4_moe_layer",
+    "nvfp4_gemm_epilogue", "nvfp4_gemm_epilogue_wait_limit", "nvfp4_linear_fprop_epilogue",
+    "nvfp4_epilogue_backward_workspace_bytes", "nvfp4_epilogue_backward", "nvfp4_adamw", "nvfp4_moe_layer_workspace_bytes", "nvfp4_moe_layer",
 )
 
 
@@ -142,6 +142,8 @@ def load(path: str = LIB_PATH):
         "nvfp4_moe_grouped_wgrad": (ci, [vp, vp, ci, i64, i64, vp, sz, vp]),
         "nvfp4_gemm_epilogue": (ci, [vp, vp, vp, vp, vp, vp, f32, i64, i64, i64, C.POINTER(Epilogue),
                                      vp, vp, vp, vp]),
+        "nvfp4_gemm_epilogue_wait_limit": (ci, [vp, vp, vp, vp, vp, vp, f32, i64, i64, i64,
+                                                C.POINTER(Epilogue), vp, vp, vp, C.c_longlong, vp]),
         "nvfp4_linear_fprop_epilogue": (ci, [vp, vp, vp, i64, i64, i64, vp, C.POINTER(LinearOpts),
                                              C.POINTER(Epilogue), vp, sz, vp]),
         "nvfp4_epilogue_backward_workspace_bytes": (sz, [i64, i64]),
@@ -517,6 +519,17 @@ def nvfp4_gemm_epilogue(A, sfA, B, sfB, alpha, M, N, K, D_bf16=None, D_f32=None,
         C.byref(e), _arg("D_bf16", D_bf16, torch.bfloat16, dev, (M, N)), _arg("D_f32", D_f32, f32, dev, (M, N)),
         _arg("status", status, torch.int32, dev, None, 1), st)
     _check("nvfp4_gemm_epilogue", rc)
+
+
+def nvfp4_gemm_epilogue_wait_limit(A, sfA, B, sfB, alpha, M, N, K, wait_cycles, D_bf16=None, D_f32=None,
+                                   scale_a=None, scale_b=None, bias=None, act=ACT_NONE, residual=None, Z=None,
+                                   status=None, stream=None):
+    """nvfp4_gemm_epilogue with the waits bounded by `wait_cycles` clock cycles (a testing hook
+    of the timeout path; 0 selects the default bound)."""
+    e = Epilogue(_ptr(bias), act, _ptr(residual), _ptr(Z))
+    _check("nvfp4_gemm_epilogue_wait_limit", load().nvfp4_gemm_epilogue_wait_limit(
+        _ptr(A), _ptr(sfA), _ptr(B), _ptr(sfB), _ptr(scale_a), _ptr(scale_b), float(alpha), M, N, K, C.byref(e),
+        _ptr(D_bf16), _ptr(D_f32), _ptr(status), int(wait_cycles), _stream(stream)))
 
 
 def nvfp4_linear_fprop_epilogue(X, W, Y, rht_signs, ws, bias=None, act=ACT_NONE, residual=None,

@@ -372,14 +372,22 @@ int nvfp4_gemm_epilogue(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, 
                         const float* scale_a, const float* scale_b, float alpha, int64_t M, int64_t N,
                         int64_t K, const nvfp4_epilogue* epi, void* D_bf16, float* D_f32, int* status,
                         nvfp4_stream_t stream) {
+    return nvfp4_gemm_epilogue_wait_limit(A, sfA, B, sfB, scale_a, scale_b, alpha, M, N, K, epi, D_bf16, D_f32, status,
+                                          0, stream);
+}
+
+int nvfp4_gemm_epilogue_wait_limit(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
+                                   const float* scale_a, const float* scale_b, float alpha, int64_t M,
+                                   int64_t N, int64_t K, const nvfp4_epilogue* epi, void* D_bf16,
+                                   float* D_f32, int* status, long long wait_cycles, nvfp4_stream_t stream) {
     NVFP4_RANGE("nvfp4_gemm_epilogue");
-    if (!epi) return NVFP4_ERR_ARG;
+    if (!epi || wait_cycles < 0) return NVFP4_ERR_ARG;
     int rc = epi_check(epi);
     if (rc) return rc;
     int sms = 0;
     if ((rc = gemm_check(A, sfA, B, sfB, M, N, K, D_bf16, D_f32, &sms))) return rc;
     return gemm_call(A, sfA, B, sfB, scale_a, scale_b, alpha, M, N, K, D_bf16, D_f32, status, sms,
-                     reinterpret_cast<cudaStream_t>(stream), 0, epi);
+                     reinterpret_cast<cudaStream_t>(stream), wait_cycles, epi);
 }
 
 size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N) {

@@ -380,10 +380,11 @@ __device__ __forceinline__ void tmem_ld_64cols(uint32_t taddr, uint32_t (&r)[64]
 
 // What an epilogue warp of the fused kernels works with: its staging buffer (32 rows of
 // CH bf16), the barrier of its residual copies and their phase, the maps of its tensors
-// in boxes of CH columns x 32 rows.
+// in boxes of CH columns x 32 rows, its CTA's timeout flag.
 struct EpiCtx {
     uint32_t buf, bar, phase;
     const CUtensorMap *tmD, *tmZ, *tmR;
+    int* timed_out;
 };
 // Start the copy of a residual box into the staging buffer, once every lane has read the
 // box before it (without a bf16 output no store's barrier comes between) and the previous
@@ -408,7 +409,9 @@ __device__ __forceinline__ void residual_fetch(const EpiCtx& x, int64_t col, int
 // (j ^ ((row / 4) % 2)).  A residual box is fetched into the buffer, read, and its place
 // taken by D's; without Z it is fetched ahead, with Z after the buffer has carried Z's
 // box.  Without HOLD (M <= 128, few tiles) CH columns at a time are drained and
-// finished.  `skip`: a timeout, the accumulator is neither read nor stored.
+// finished.  `skip`: a timeout, the accumulator is neither read nor stored.  A residual
+// wait that runs out sets the flag and then lets the box land (no copy of its own outlives
+// the warp, nothing is made of an older box).
 // Without Z the caller has started the tile's first residual box.
 template <int CW, int CH, bool HOLD>
 __device__ __forceinline__ void epilogue_fused(uint32_t lane_base, int64_t row0, int64_t col0, const GemmParams& p,
@@ -477,7 +480,10 @@ __device__ __forceinline__ void epilogue_fused(uint32_t lane_base, int64_t row0,
             default: break;
         }
         if (p.residual) {
-            if (!mbar_wait(x.bar, x.phase, kWaitCycles)) set_status(p.status, kStatusTimeout);
+            if (!mbar_wait(x.bar, x.phase, p.wait_cycles > 0 ? p.wait_cycles : kWaitCycles)) {
+                *x.timed_out = 1;
+                mbar_wait_drain(x.bar, x.phase);
+            }
             x.phase ^= 1u;
 #pragma unroll
             for (int j = 0; j < CH / 8; ++j) {
@@ -518,7 +524,7 @@ __device__ __forceinline__ void epilogue_fused(uint32_t lane_base, int64_t row0,
     if (skip) {
         release();
         if (p.residual && !p.Z && store && col0 < p.N) {  // the box that was started lands all the same
-            (void)mbar_wait(x.bar, x.phase, kWaitCycles);
+            mbar_wait_drain(x.bar, x.phase);
             x.phase ^= 1u;
         }
         return;
@@ -797,9 +803,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         constexpr int HC = BN / 2;               // columns per epilogue warp
         const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * HC);
         uint32_t local = 0;
-        EpiCtx ctx{smem_addr(S.dstage[warp - 6]), smem_addr(&S.res_full[warp - 6]), 0u, &tmD, &tmZ, &tmR};
+        EpiCtx ctx{smem_addr(S.dstage[warp - 6]), smem_addr(&S.res_full[warp - 6]), 0u, &tmD, &tmZ, &tmR, &timed_out};
         for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++local) {
-            if (*(volatile int*)&timed_out) break;  // a stage failed: no further tiles arrive
+            // a stage failed: no further tiles arrive (the whole warp leaves, or none)
+            if (__any_sync(0xFFFFFFFFu, *(volatile int*)&timed_out)) break;
             const TileJob jb = tile_job<BN>(p, tile, tiles_n, tiles_per_group);
             float alpha = p.alpha;
             const int gs = jb.group < 0 ? 0 : jb.group;
@@ -814,7 +821,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             __syncwarp();
             if (!acc_ok) timed_out = 1;
             // after a timeout the accumulator is neither read nor stored
-            const bool bad = *(volatile int*)&timed_out != 0;
+            const bool bad = __any_sync(0xFFFFFFFFu, !acc_ok || *(volatile int*)&timed_out);
             const int64_t m_in = (jb.d_row - (jb.group >= 0 && p.group_mode == 2 ? (int64_t)jb.group * p.M : 0)) + 32 * q;
             if constexpr (kEpi)
                 epilogue_fused<HC, 16, false>(lane_base, jb.d_row + 32 * q, jb.n0 + half * HC, p, alpha,
@@ -1328,9 +1335,9 @@ __global__ void __launch_bounds__(pair_threads<EW>(), 1)
         const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(part * kEpiCols);
         const uint32_t acc_empty_l = leader ? smem_addr(&S.acc_empty) : mapa_shared(smem_addr(&S.acc_empty), 0);
         uint32_t local = 0;
-        EpiCtx ctx{smem_addr(S.dstage[warp - 6]), smem_addr(&S.res_full[warp - 6]), 0u, &tmD, &tmZ, &tmR};
+        EpiCtx ctx{smem_addr(S.dstage[warp - 6]), smem_addr(&S.res_full[warp - 6]), 0u, &tmD, &tmZ, &tmR, &timed_out};
         for (int64_t pt = cid; pt < tiles; pt += ncl, ++local) {
-            if (*(volatile int*)&timed_out) break;
+            if (__any_sync(0xFFFFFFFFu, *(volatile int*)&timed_out)) break;
             const PairJob jb = job_of(pt);
             float alpha = p.alpha;
             const int gs = jb.group < 0 ? 0 : jb.group;
@@ -1345,7 +1352,7 @@ __global__ void __launch_bounds__(pair_threads<EW>(), 1)
             __syncwarp();
             if (!acc_ok) timed_out = 1;
             // after a timeout the accumulator is neither read nor stored
-            const bool bad = *(volatile int*)&timed_out != 0;
+            const bool bad = __any_sync(0xFFFFFFFFu, !acc_ok || *(volatile int*)&timed_out);
             const int64_t r_in = 128 * rank + 32 * q;  // this warp's first row inside the tile
             if constexpr (kEpi)
                 epilogue_fused<kEpiCols, 32, true>(lane_base, jb.d_row + r_in, jb.n0 + part * kEpiCols, p, alpha,

@@ -348,9 +348,9 @@ enum { NVFP4_ACT_NONE = 0, NVFP4_ACT_RELU2 = 1, NVFP4_ACT_GELU = 2, NVFP4_ACT_SI
  *     bias      nullable device fp32 [N].
  *     act       NVFP4_ACT_*.
  *     residual  nullable device bf16 [M][N], added after the activation.  It may be
- *               D_bf16 itself (updated in place); other overlaps are not allowed.
+ *               D_bf16 itself (updated in place).
  *     Z         nullable out, bf16 [M][N]: z rounded, what nvfp4_epilogue_backward needs.
- *               Not with an overlap of another tensor.
+ *   No output may overlap another tensor otherwise (NVFP4_ERR_ARG).
  *   The other arguments, layouts and limits are nvfp4_gemm's.  With no bias, no
  *   activation, no residual and no Z the outputs equal nvfp4_gemm's.
  */

@@ -37,7 +37,8 @@ EXPORTS = (
     "nvfp4_moe_grouped_dgrad", "nvfp4_moe_grouped_wgrad", "nvfp4_gemm_wait_limit",
     "nvfp4_moe_grouped_fprop_gather",
     "nvfp4_gemm_epilogue", "nvfp4_gemm_epilogue_wait_limit", "nvfp4_linear_fprop_epilogue",
-    "nvfp4_epilogue_backward_workspace_bytes", "nvfp4_epilogue_backward", "nvfp4_adamw", "nvfp4_moe_layer_workspace_bytes", "nvfp4_moe_layer",
+    "nvfp4_epilogue_backward_workspace_bytes", "nvfp4_epilogue_backward", "nvfp4_adamw",
+    "nvfp4_moe_layer_workspace_bytes", "nvfp4_moe_layer",
 )
 
 

@@ -10,6 +10,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "../../include/nvfp4.h"
 #include "internal.h"
 
@@ -58,6 +60,29 @@ int device_check(int* sm_count) {
     if (d.status < 0) return NVFP4_ERR_DEVICE;
     *sm_count = d.sm_count;
     return NVFP4_OK;
+}
+
+// Memory that a call writes or reads (null: none).
+struct Range {
+    const void* p;
+    uint64_t bytes;
+};
+uint64_t bytes_of(int64_t rows, int64_t cols, int64_t size) {  // sizes past any memory do not wrap
+    return (double)rows * (double)cols * (double)size > 0x1p60 ? 1ull << 60 : (uint64_t)rows * (uint64_t)cols * (uint64_t)size;
+}
+// Whether an output shares memory with another output or with an input.
+bool outputs_overlap(std::initializer_list<Range> out, std::initializer_list<Range> in) {
+    auto meet = [](const Range& a, const Range& b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return x && y && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+    };
+    for (const Range* a = out.begin(); a != out.end(); ++a) {
+        for (const Range* b = a + 1; b != out.end(); ++b)
+            if (meet(*a, *b)) return true;
+        for (const Range& b : in)
+            if (meet(*a, b)) return true;
+    }
+    return false;
 }
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
@@ -166,15 +191,30 @@ int gemm_call(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint
     return cuda_status(launch_gemm(g, sms, st));
 }
 
-// Host checks of a dense GEMM, before anything is launched.
-int gemm_check(const void* A, const void* sfA, const void* B, const void* sfB, int64_t M, int64_t N, int64_t K,
-               const void* D_bf16, const void* D_f32, int* sms) {
+// Host checks of a dense GEMM, before anything is launched.  With an epilogue also that no
+// output overlaps another tensor, but for a residual updated in place.
+int gemm_check(const void* A, const void* sfA, const void* B, const void* sfB, const float* scale_a,
+               const float* scale_b, int64_t M, int64_t N, int64_t K, const nvfp4_epilogue* e, const void* D_bf16,
+               const void* D_f32, const int* status, int* sms) {
     if (!A || !sfA || !B || !sfB || (!D_bf16 && !D_f32)) return NVFP4_ERR_ARG;
     if (M < 1 || N < 8 || K < 64 || K % 64 != 0 || N % 8 != 0) return NVFP4_ERR_SHAPE;
     if (M > (1ll << 31) - 256 || N > (1ll << 31) - 256 || K / 2 > (1ll << 31)) return NVFP4_ERR_SHAPE;
     if (!aligned(A, 16) || !aligned(B, 16) || !aligned(sfA, 16) || !aligned(sfB, 16) ||
         (D_bf16 && !aligned(D_bf16, 16)) || (D_f32 && !aligned(D_f32, 16)))
         return NVFP4_ERR_ALIGN;
+    if (e) {
+        const uint64_t half = bytes_of(M, N, 2);
+        if (outputs_overlap({{D_bf16, half}, {D_f32, bytes_of(M, N, 4)}, {e->Z, half}, {status, 4}},
+                            {{e->residual == D_bf16 ? nullptr : e->residual, half},
+                             {e->bias, bytes_of(N, 1, 4)},
+                             {A, bytes_of(M, K / 2, 1)},
+                             {B, bytes_of(N, K / 2, 1)},
+                             {sfA, nvfp4_scale_bytes(M, K)},
+                             {sfB, nvfp4_scale_bytes(N, K)},
+                             {scale_a, 4},
+                             {scale_b, 4}}))
+            return NVFP4_ERR_ARG;
+    }
     return device_check(sms);
 }
 
@@ -362,7 +402,7 @@ int nvfp4_gemm_wait_limit(const uint8_t* A, const uint8_t* sfA, const uint8_t* B
     NVFP4_RANGE("nvfp4_gemm_wait_limit");
     if (wait_cycles < 0) return NVFP4_ERR_ARG;
     int sms = 0;
-    int rc = gemm_check(A, sfA, B, sfB, M, N, K, D_bf16, D_f32, &sms);
+    int rc = gemm_check(A, sfA, B, sfB, scale_a, scale_b, M, N, K, nullptr, D_bf16, D_f32, status, &sms);
     if (rc) return rc;
     return gemm_call(A, sfA, B, sfB, scale_a, scale_b, alpha, M, N, K, D_bf16, D_f32, status, sms,
                      reinterpret_cast<cudaStream_t>(stream), wait_cycles);
@@ -385,7 +425,7 @@ int nvfp4_gemm_epilogue_wait_limit(const uint8_t* A, const uint8_t* sfA, const u
     int rc = epi_check(epi);
     if (rc) return rc;
     int sms = 0;
-    if ((rc = gemm_check(A, sfA, B, sfB, M, N, K, D_bf16, D_f32, &sms))) return rc;
+    if ((rc = gemm_check(A, sfA, B, sfB, scale_a, scale_b, M, N, K, epi, D_bf16, D_f32, status, &sms))) return rc;
     return gemm_call(A, sfA, B, sfB, scale_a, scale_b, alpha, M, N, K, D_bf16, D_f32, status, sms,
                      reinterpret_cast<cudaStream_t>(stream), wait_cycles, epi);
 }
@@ -443,6 +483,13 @@ static int linear_fprop(const void* X, const void* W, void* Y, int64_t M, int64_
     const int dgrad_rht = opts ? opts->dgrad_rht : 0;
     if ((rc = lin_check(M, K, N, ws, ws_bytes))) return rc;
     if (!aligned(X, 16) || !aligned(W, 16) || !aligned(Y, 16)) return NVFP4_ERR_ALIGN;
+    if (epi) {
+        const uint64_t out = bytes_of(M, N, 2);
+        if (outputs_overlap({{Y, out}, {epi->Z, out}, {ws, nvfp4_linear_workspace_bytes(M, K, N)}},
+                            {{epi->residual == Y ? nullptr : epi->residual, out}, {epi->bias, bytes_of(N, 1, 4)}}) ||
+            outputs_overlap({{epi->Z, out}}, {{X, bytes_of(M, K, 2)}, {W, bytes_of(N, K, 2)}}))
+            return NVFP4_ERR_ARG;
+    }
     int sms = 0;
     if ((rc = device_check(&sms))) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -412,8 +412,8 @@ int nvfp4_epilogue_backward(const void* dY, const void* Z, int act, int64_t M, i
  *             neighbours); a sqrt(v) above zero does not become zero.  A block that
  *             holds Inf or NaN becomes NaN (scale 255).
  *     n       elements, 0 allowed (skipped), up to 2^40.      weight_decay  wd.
- *     p, grad, w_bf16, m and v 16-byte aligned.  The ranges of p must not overlap
- *     between entries (NVFP4_ERR_ARG); the other buffers must not either.
+ *     p, grad, w_bf16, m and v 16-byte aligned.  What the step writes must not overlap
+ *     anything else in the list (NVFP4_ERR_ARG); gradients may share memory.
  *   opts (host)
  *     lr >= 0 and finite, 0 <= beta1, beta2 < 1, 2^-126 <= eps < 2^126, step t >= 1 (the
  *     first step is 1).  Each wd >= 0 and finite.

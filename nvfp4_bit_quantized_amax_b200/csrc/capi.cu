@@ -6,10 +6,12 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <nvtx3/nvToolsExt.h>
+#include <stddef.h>
 #include <stdint.h>
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <initializer_list>
 
 #include "../../include/nvfp4.h"
@@ -1093,36 +1095,89 @@ MoeLayerLayout moe_layer_layout(int64_t T, int topk, int64_t K, int64_t F) {
     L.total = off;
     return L;
 }
-// Whether two tensors' fp32 parameters share memory (a list that names one twice).
+// Whether memory that a step writes (parameters, copies, moments, scales) is named a second
+// time, as another output or as a gradient.  Gradients may be shared.  Parts of one flat buffer
+// per kind, in order and apart, are seen at once (300 tensors of 7 buffers: 4 us); else the
+// buffers are walked in the order of their addresses, which within a kind mostly is the
+// list's already (17 us), or they are sorted (25 to 40 us).
 struct Span {
     uintptr_t lo, hi;
+    bool written;
 };
-int adamw_overlap(const nvfp4_adamw_tensor* t, int count, bool* overlap) {
+struct SpanWalk {
+    uintptr_t end = 0, end_written = 0;
+    bool overlap = false;
+    void visit(const Span& s) {
+        overlap |= s.lo < (s.written ? end : end_written);
+        end = std::max(end, s.hi);
+        if (s.written) end_written = std::max(end_written, s.hi);
+    }
+};
+int adamw_overlap(const nvfp4_adamw_tensor* t, int count, const nvfp4_adamw_opts* o, bool* overlap) {
+    constexpr int kKinds = 7, kGrad = 1;
+    const int kinds = o->state_bits == 8 ? 7 : 5;
+    const uint64_t state = o->state_bits == 8 ? 1 : 4;
+    const uint64_t size[kKinds] = {4, o->grad_f32 ? 4u : 2u, 2, state, state, 0, 0};
+    auto span = [&](int i, int kind) -> Span {
+        // an entry begins with its seven pointers, in this order
+        static_assert(offsetof(nvfp4_adamw_tensor, grad) == 8 && offsetof(nvfp4_adamw_tensor, v_scale) == 48, "");
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(reinterpret_cast<const void* const*>(t + i)[kind]);
+        const uint64_t n = (uint64_t)t[i].n, bytes = kind < 5 ? n * size[kind] : (n + 31) / 32;
+        return {lo, lo ? lo + bytes : 0, kind != kGrad};
+    };
+    Span hull[kKinds];
+    bool flat = true;
+    for (int kind = 0; kind < kinds && flat; ++kind) {
+        uintptr_t first = UINTPTR_MAX, last = 0;
+        for (int i = 0; i < count; ++i) {
+            const Span s = span(i, kind);
+            if (s.lo == s.hi) continue;
+            flat &= s.lo >= last;
+            first = std::min(first, s.lo);
+            last = s.hi;
+        }
+        hull[kind] = {first, last, true};
+        for (int k = 0; k < kind; ++k) flat &= hull[k].hi <= first || last <= hull[k].lo;
+    }
     *overlap = false;
-    uintptr_t end = 0;
-    bool ascending = true;  // the usual list: in address order already
-    for (int i = 0; i < count && ascending; ++i) {
-        if (t[i].n == 0) continue;
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(t[i].p);
-        if (lo < end) ascending = false;
-        end = lo + 4 * (uintptr_t)t[i].n;
+    if (flat) return NVFP4_OK;
+    Span head[kKinds];
+    int next[kKinds] = {};
+    bool ordered = true;
+    auto advance = [&](int kind) {  // this kind's next buffer; past the last one an empty span at the end
+        const uintptr_t before = head[kind].lo;
+        do head[kind] = next[kind] < count ? span(next[kind]++, kind) : Span{UINTPTR_MAX, UINTPTR_MAX, false};
+        while (head[kind].lo == head[kind].hi && head[kind].lo != UINTPTR_MAX);
+        ordered &= head[kind].lo >= before;
+    };
+    for (int kind = 0; kind < kinds; ++kind) {
+        head[kind].lo = 0;
+        advance(kind);
     }
-    if (ascending) return NVFP4_OK;
-    Span* s = static_cast<Span*>(malloc(sizeof(Span) * (size_t)count));
-    if (!s) return NVFP4_ERR_ARG;
-    int k = 0;
-    for (int i = 0; i < count; ++i) {
-        if (t[i].n == 0) continue;
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(t[i].p);
-        s[k++] = {lo, lo + 4 * (uintptr_t)t[i].n};
+    SpanWalk walk;
+    while (ordered) {
+        int low = 0;
+        for (int kind = 1; kind < kinds; ++kind)
+            if (head[kind].lo < head[low].lo) low = kind;
+        if (head[low].lo == UINTPTR_MAX) break;
+        walk.visit(head[low]);
+        advance(low);
     }
-    qsort(s, (size_t)k, sizeof(Span), [](const void* a, const void* b) {
-        const uintptr_t x = static_cast<const Span*>(a)->lo, y = static_cast<const Span*>(b)->lo;
-        return x < y ? -1 : x > y ? 1 : 0;
-    });
-    for (int i = 1; i < k; ++i)
-        if (s[i].lo < s[i - 1].hi) *overlap = true;
-    free(s);
+    if (!ordered) {
+        Span* s = static_cast<Span*>(malloc(sizeof(Span) * (size_t)count * kKinds));
+        if (!s) return NVFP4_ERR_ARG;
+        size_t k = 0;
+        for (int i = 0; i < count; ++i)
+            for (int kind = 0; kind < kinds; ++kind) {
+                s[k] = span(i, kind);
+                if (s[k].lo != s[k].hi) ++k;
+            }
+        std::sort(s, s + k, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+        walk = SpanWalk{};
+        for (size_t i = 0; i < k; ++i) walk.visit(s[i]);
+        free(s);
+    }
+    *overlap = walk.overlap;
     return NVFP4_OK;
 }
 }  // namespace
@@ -1179,7 +1234,7 @@ int nvfp4_adamw(const nvfp4_adamw_tensor* tensors, int count, const nvfp4_adamw_
             return NVFP4_ERR_ALIGN;
     }
     bool overlap = false;
-    int rc = adamw_overlap(tensors, count, &overlap);
+    int rc = adamw_overlap(tensors, count, o, &overlap);
     if (rc) return rc;
     if (overlap) return NVFP4_ERR_ARG;
     int sms = 0;

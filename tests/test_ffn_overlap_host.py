@@ -86,3 +86,66 @@ def test_linear_fprop_epilogue(lib):
     assert call(at) == capi.ERR_CUDA
     at["Y"] = at["res"] = at["X"]  # the input is in the workspace before Y is written
     assert call(at) == call(at, False) == capi.ERR_CUDA
+
+
+NAMES = "p grad w m v m_scale v_scale"
+
+
+def adamw(lib, entries, bits, grad_f32=0):
+    arr = (capi.AdamWTensor * len(entries))(*[capi.AdamWTensor(*e) for e in entries])
+    o = capi.AdamWOpts(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, step=1, seed=0, state_bits=bits, grad_f32=grad_f32)
+    return lib.nvfp4_adamw(arr, len(entries), C.byref(o), None)
+
+
+def entry(base, n, bits):
+    """One tensor whose buffers lie 64 MB apart from `base` on."""
+    at = {x: base + i * 64 * MB for i, x in enumerate(NAMES.split())}
+    if bits == 32:
+        at["m_scale"] = at["v_scale"] = None
+    return dict(at, n=n, wd=0.0)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("order", ["ascending", "descending"])
+def test_adamw(lib, bits, order):
+    """Every pair of buffers, inside a tensor and between two: what is written may not be named
+    twice, gradients may."""
+    n = 1000
+    state, sc = (4, 0) if bits == 32 else (1, (n + 31) // 32)
+    size = dict(p=4 * n, grad=2 * n, w=2 * n, m=state * n, v=state * n, m_scale=sc, v_scale=sc)
+    bases = [4096 * MB, 8192 * MB, 12288 * MB]
+    bases = bases if order == "ascending" else bases[::-1]
+    kinds = [k for k in NAMES.split() if size[k]]
+
+    def call(change=None):
+        e = [entry(b, n, bits) for b in bases]
+        e.insert(1, entry(bases[0], 0, bits))  # an empty tensor names memory, but touches none
+        if change:
+            (i, a), (j, b), d = change
+            e[i][a] = e[j][b] + d
+        return adamw(lib, [tuple(x.values()) for x in e], bits)
+    assert call() == capi.ERR_CUDA  # no device: accepted
+    for i, j in ((0, 0), (0, 2), (3, 2), (2, 0)):
+        for a in kinds:
+            for b in kinds:
+                if (i, a) == (j, b):
+                    continue
+                for d in (0, size[b] // 16 * 16 - 16, 16 - size[a] // 16 * 16):
+                    if not -size[a] < d < size[b]:
+                        continue
+                    want = capi.ERR_CUDA if a == b == "grad" else capi.ERR_ARG
+                    assert call(((i, a), (j, b), d)) == want, (i, a, j, b, d)
+                # directly behind it
+                assert call(((i, a), (j, b), (size[b] + 15) // 16 * 16)) == capi.ERR_CUDA, (i, a, j, b)
+
+
+def test_adamw_parts_of_one_buffer_per_kind(lib):
+    """An optimizer's flat buffers: neighbouring parts, in and out of order."""
+    for order in (range(50), reversed(range(50)), [(i * 7) % 50 for i in range(50)]):
+        e = []
+        for i in order:
+            at = entry(4096 * MB, 128, 8)
+            e.append(tuple(at[k] + i * s for k, s in zip(NAMES.split(), (512, 256, 256, 128, 128, 4, 4))) + (128, 0.0))
+        assert adamw(lib, e, 8) == capi.ERR_CUDA
+        e[31] = e[31][:3] + (e[30][3],) + e[31][4:]  # one m named twice
+        assert adamw(lib, e, 8) == capi.ERR_ARG

@@ -381,7 +381,8 @@ int nvfp4_linear_fprop_epilogue(const void* X, const void* W, void* Y, int64_t M
 /*
  * nvfp4_epilogue_backward -- dZ = dY act'(Z), dbias[n] = sum over m of the unrounded dZ
  * (the residual's gradient is dY).
- *   dY, Z, dZ  bf16 [M][N]; dZ may be dY or Z (updated in place), no other overlap.
+ *   dY, Z, dZ  bf16 [M][N]; dZ may be dY or Z (updated in place).  No other overlap of an
+ *              output, the workspace among them (NVFP4_ERR_ARG).
  *   dbias      nullable out, fp32 [N].
  *   workspace  nvfp4_epilogue_backward_workspace_bytes(M, N) bytes, 16-byte aligned;
  *              may be NULL without dbias or where that is 0.  Scratch of one call: calls

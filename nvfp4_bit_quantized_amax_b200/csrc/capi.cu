@@ -1199,6 +1199,10 @@ int nvfp4_epilogue_backward(const void* dY, const void* Z, int act, int64_t M, i
     const size_t need = dbias ? nvfp4_epilogue_backward_workspace_bytes(M, N) : 0;
     if (need && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
     if (need && !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
+    const uint64_t b = bytes_of(M, N, 2);
+    if (outputs_overlap({{dZ, b}, {dbias, bytes_of(N, 1, 4)}, {need ? workspace : nullptr, need}},
+                        {{dY == dZ ? nullptr : dY, b}, {Z == dZ ? nullptr : Z, b}}))
+        return NVFP4_ERR_ARG;
     int sms = 0;
     const int rc = device_check(&sms);
     if (rc) return rc;

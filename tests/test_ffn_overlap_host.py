@@ -149,3 +149,29 @@ def test_adamw_parts_of_one_buffer_per_kind(lib):
         assert adamw(lib, e, 8) == capi.ERR_CUDA
         e[31] = e[31][:3] + (e[30][3],) + e[31][4:]  # one m named twice
         assert adamw(lib, e, 8) == capi.ERR_ARG
+
+
+def test_epilogue_backward(lib):
+    m, n = 500, 264
+    ws = capi.epilogue_backward_workspace_bytes(m, n)
+    size = dict(dY=2 * m * n, Z=2 * m * n, dZ=2 * m * n, db=4 * n, ws=ws)
+
+    def call(at, dbias=True):
+        return lib.nvfp4_epilogue_backward(at["dY"], at["Z"], capi.ACT_GELU, m, n, at["dZ"], at["db"] if dbias else None,
+                                           at["ws"], ws, None)
+    for a in ("dZ", "db", "ws"):
+        for b in size:
+            if a == b:
+                continue
+            for d in distances(size[a], size[b]):
+                at = places("dY Z dZ db ws")
+                at[b] = at[a] + d
+                if at[b] % 16:
+                    continue
+                meets = -size[b] < d < size[a] and not (a == "dZ" and b in ("dY", "Z") and d == 0)
+                assert call(at) == (capi.ERR_ARG if meets else capi.ERR_CUDA), (a, b, d)
+                if "ws" in (a, b):  # without sums the workspace is not touched
+                    assert call(at, dbias=False) == capi.ERR_CUDA
+    at = places("dY Z dZ db ws")
+    at["Z"] = at["dZ"] = at["dY"]
+    assert call(at) == capi.ERR_CUDA

@@ -455,7 +455,8 @@ int nvfp4_adamw(const nvfp4_adamw_tensor* tensors, int count, const nvfp4_adamw_
  *   w = s of the chosen (divided by their sum if renormalize) * route_scale;
  *   h_e = act(g1_e W1_e x), or gated: act(first F rows) * (last F rows);
  *   y = sum over the chosen of w_e g2_e W2_e h_e.
- *   X [tokens][K], router [E][K], Y [tokens][K]  bf16; Y may be X.
+ *   X [tokens][K], router [E][K], Y [tokens][K]  bf16; Y may be X.  No other
+ *        overlap of an output, the workspace among them (NVFP4_ERR_ARG).
  *   W1   [E * F (1 + gated)][K], W2 [E * K][F]: quantized operands with one tensor scale
  *        per expert (as nvfp4_moe_grouped_operand's NVFP4_LIN_W_ROW views; any block
  *        mode).  rows and cols must say those sizes.

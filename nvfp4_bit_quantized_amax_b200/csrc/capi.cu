@@ -1284,11 +1284,23 @@ int nvfp4_moe_layer(const void* X, const void* router, const nvfp4_tensor* W1, c
         (o->select_bias && !aligned(o->select_bias, 4)) || (o->topk_idx && !aligned(o->topk_idx, 4)) ||
         (o->topk_weight && !aligned(o->topk_weight, 4)))
         return NVFP4_ERR_ALIGN;
-    if (!ws || ws_bytes < nvfp4_moe_layer_workspace_bytes(tokens, E, topk, K, F)) return NVFP4_ERR_WORKSPACE;
+    const MoeLayerLayout L = moe_layer_layout(tokens, topk, K, F);
+    if (!ws || ws_bytes < (size_t)L.total) return NVFP4_ERR_WORKSPACE;
+    const uint64_t row = bytes_of(tokens, K, 2), choice = bytes_of(tokens, topk, 4), e4 = bytes_of(E, 1, 4);
+    if (outputs_overlap({{Y, row}, {ws, (uint64_t)L.total}, {o->topk_idx, choice}, {o->topk_weight, choice}},
+                        {{X == Y ? nullptr : X, row},
+                         {router, bytes_of(E, K, 2)},
+                         {o->select_bias, e4},
+                         {W1->data, bytes_of(W1->rows, K / 2, 1)},
+                         {W1->scales, nvfp4_scale_bytes(W1->rows, K)},
+                         {W1->tensor_scale, e4},
+                         {W2->data, bytes_of(W2->rows, F / 2, 1)},
+                         {W2->scales, nvfp4_scale_bytes(W2->rows, F)},
+                         {W2->tensor_scale, e4}}))
+        return NVFP4_ERR_ARG;
     int sms = 0;
     const int rc = device_check(&sms);
     if (rc) return rc;
-    const MoeLayerLayout L = moe_layer_layout(tokens, topk, K, F);
     uint8_t* b = static_cast<uint8_t*>(ws);
     MoeLayerParams p{};
     p.x = static_cast<const uint16_t*>(X);

@@ -175,3 +175,36 @@ def test_epilogue_backward(lib):
     at = places("dY Z dZ db ws")
     at["Z"] = at["dZ"] = at["dY"]
     assert call(at) == capi.ERR_CUDA
+
+
+def test_moe_layer(lib):
+    t, e, topk, k, f = 7, 10, 3, 640, 384
+    ws = capi.moe_layer_workspace_bytes(t, e, topk, k, f)
+    r1, r2 = e * 2 * f, e * k
+    size = dict(x=2 * t * k, router=2 * e * k, y=2 * t * k, bias=4 * e, idx=4 * t * topk, weight=4 * t * topk, ws=ws,
+                d1=r1 * k // 2, s1=capi.scale_bytes(r1, k), g1=4 * e, d2=r2 * f // 2, s2=capi.scale_bytes(r2, f), g2=4 * e)
+    names = " ".join(size)
+
+    def call(at):
+        o = capi.MoeLayerOpts(capi.ACT_SILU, 1, 0, 1, 1.0, at["bias"], at["idx"], at["weight"])
+        return lib.nvfp4_moe_layer(at["x"], at["router"], C.byref(capi.Tensor(at["d1"], at["s1"], at["g1"], r1, k)),
+                                   C.byref(capi.Tensor(at["d2"], at["s2"], at["g2"], r2, f)), at["y"], t, e, topk, k, f,
+                                   C.byref(o), at["ws"], ws, None)
+    assert call(places(names)) == capi.ERR_CUDA
+    for a in ("y", "ws", "idx", "weight"):
+        for b in size:
+            if a == b:
+                continue
+            for d in distances(size[a], size[b]):
+                d = d // 256 * 256 if "ws" in (a, b) else d  # the workspace's alignment
+                at = places(names)
+                at[b] = at[a] + d
+                if at[b] % 16:
+                    continue
+                meets = -size[b] < d < size[a] and not ({a, b} == {"x", "y"} and d == 0)
+                assert call(at) == (capi.ERR_ARG if meets else capi.ERR_CUDA), (a, b, d)
+    at = places(names)
+    at["y"] = at["x"]
+    assert call(at) == capi.ERR_CUDA
+    at["idx"] = at["x"] + 64
+    assert call(at) == capi.ERR_ARG

@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
 #include <cmath>
 
 #include "activation.cuh"
@@ -50,6 +51,12 @@ __device__ __forceinline__ void store_remote_f64(const void* local, uint32_t cta
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
+// An integer whose order is the number's, both zeros alike, NaN below -infinity.
+__device__ __forceinline__ long long order_of(double v) {
+    const long long b = __double_as_longlong(v + 0.0);
+    return v != v ? LLONG_MIN : b < 0 ? b ^ LLONG_MAX : b;
+}
+
 // A cluster takes TC tokens.  Logits: a warp takes an expert and the cluster's tokens;
 // products of eight elements are added in fp32, those sums in fp64, so that the choice
 // does not hang on the order of the additions or on the batch.  The logits of token r go
@@ -59,7 +66,7 @@ template <int TC>
 __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteThreads)
     moe_route_kernel(const MoeLayerParams p) {
     __shared__ double logit[kMaxGroups];
-    __shared__ double key[kMaxGroups];
+    __shared__ long long key[kMaxGroups];
     __shared__ int chosen[kMoeMaxTopk];
     __shared__ double red[kRouteWarps];
     __shared__ uint32_t amax;
@@ -145,14 +152,14 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
         double k = logit[e];
         if (p.sel_bias != nullptr)
             k = (p.sigmoid ? 1.0 / (1.0 + exp(-k)) : exp(k - top) / sum) + (double)p.sel_bias[e];
-        key[e] = k == k ? k : -INFINITY;
+        key[e] = order_of(k);
     }
     __syncthreads();
     int parts = 1;  // threads that count for one expert
     while (parts < 32 && p.E * parts * 2 <= kRouteThreads) parts *= 2;
     for (int e0 = 0; e0 < p.E; e0 += kRouteThreads / parts) {
         const int e = e0 + threadIdx.x / parts;
-        const double k = e < p.E ? key[e] : 0.0;
+        const long long k = e < p.E ? key[e] : 0;
         int place = 0;
         for (int o = threadIdx.x % parts; o < p.E; o += parts) place += key[o] > k || (key[o] == k && o < e) ? 1 : 0;
         for (int o = 1; o < parts; o <<= 1) place += __shfl_xor_sync(0xFFFFFFFFu, place, o);

@@ -148,13 +148,15 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
         for (int i = 0; i < kRouteWarps; ++i) sum += red[i];
     }
     // without a bias the logits themselves give the order
+    bool nan = false;
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
         double k = logit[e];
+        nan |= k != k;
         if (p.sel_bias != nullptr)
             k = (p.sigmoid ? 1.0 / (1.0 + exp(-k)) : exp(k - top) / sum) + (double)p.sel_bias[e];
         key[e] = order_of(k);
     }
-    __syncthreads();
+    const bool any_nan = __syncthreads_or(nan);
     int parts = 1;  // threads that count for one expert
     while (parts < 32 && p.E * parts * 2 <= kRouteThreads) parts *= 2;
     for (int e0 = 0; e0 < p.E; e0 += kRouteThreads / parts) {
@@ -188,6 +190,7 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
         } else if (!p.sigmoid) {
             s = (float)(exp(logit[e] - top) / sum);
         }
+        if (!p.sigmoid && any_nan) s = __uint_as_float(0x7FFFFFFFu);  // one NaN spoils a softmax
         p.idx[t * p.topk + j] = e;
         p.weight[t * p.topk + j] = s * p.route_scale;
     }

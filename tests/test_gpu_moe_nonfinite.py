@@ -65,3 +65,20 @@ def test_nan_comes_behind_minus_infinity_with_a_bias():
     for topk in (1, 4, 6):
         idx, _ = route(logits, topk, scoring=capi.SCORE_SIGMOID, select_bias=bias)
         assert idx[0].tolist() == order(s.tolist(), topk)
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("bias", [False, True])
+def test_one_nan_spoils_a_softmax(bias, renormalize):
+    """softmax has no value where one logit has none, whichever experts are taken; logistic
+    scores stand each for itself."""
+    logits = torch.tensor([[1.0, 3.0, NAN, 2.0], [0.5, NAN, -INF, 0.25], [1.0, 3.0, -INF, 2.0]])
+    sel = torch.zeros(4, device=DEV) if bias else None
+    idx, w = route(logits, 2, scoring=capi.SCORE_SOFTMAX, select_bias=sel, renormalize=renormalize)
+    assert w[:2].isnan().all() and w[2].isfinite().all()
+    assert idx[2].tolist() == [1, 3] and (bias or idx[:2].tolist() == [[1, 3], [0, 3]])
+    idx, w = route(logits, 2, scoring=capi.SCORE_SIGMOID, select_bias=sel, renormalize=renormalize)
+    assert w.isfinite().all() and idx.tolist() == [[1, 3], [0, 3], [1, 3]]
+    s = torch.sigmoid(logits.double()).gather(1, idx.long())
+    s = s / s.sum(1, keepdim=True) if renormalize else s
+    assert ((w.double() - s).abs() <= 2.0 ** -18 * s).all()

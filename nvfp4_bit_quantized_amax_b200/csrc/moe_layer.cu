@@ -225,6 +225,7 @@ constexpr int kMaxTiles = 4;            // 8-column tiles of one pass
 // 4096 x 2048, top 2 (7) 154 and 132.
 constexpr int kCountedItems = 12;
 constexpr int kMaxDepth = 5;            // stages of a warp's ring
+constexpr int kMoeMaxGrid = 256;        // CTAs of a projection
 constexpr int kScaleBytes = 2 * 40 * 4;  // two atoms' words of 32 rows, padded apart
 constexpr int kStageBytes = 4 * 512 + kScaleBytes;  // of one warp: 32 rows x 64 bytes, scales
 
@@ -453,8 +454,14 @@ __global__ void __launch_bounds__(kExpThreads, 1) moe_expert_kernel(const MoeLay
         }
     }
     __syncthreads();
-    // CTA b's first item: an equal share of the items, or of the experts' loads in whole tiles
-    // (32 bits hold them: 2^10 experts, 2^9 tiles, loads of 2^13 in all, some 150 CTAs)
+    // CTA b's first item: an equal share of the items, or of the experts' loads in whole tiles.
+    // 32 bits hold both products: an expert has at most F / 16 = 2^10 tiles (gated), there are
+    // 2^10 experts, and a token counts at most twice (a pass and a tile of its own), so the loads
+    // are 2^12 in all; b goes up to the grid's size.
+    static_assert((uint64_t)kMaxGroups * (kMoeMaxDim / 16) * kMoeMaxGrid < 1ull << 31 &&
+                      2ull * kMoeMaxTokens * kMoeMaxTopk * (kMoeMaxDim / 16) * kMoeMaxGrid < 1ull << 32,
+                  "the shares' products fit in 32 bits");
+    static_assert(2 * kMoeMaxTokens * kMoeMaxTopk < 1 << 16 && kMaxGroups < 1 << 16, "the lists hold 16 bits");
     auto share = [&](uint32_t b) -> int {
         if (even || b == gridDim.x) return (int)((uint32_t)(nactive * tiles) * b / gridDim.x);
         const uint32_t u = (uint32_t)load0[nactive] * (uint32_t)tiles * b / gridDim.x;
@@ -811,7 +818,7 @@ static cudaError_t launch_expert_mt(const MoeLayerParams& p, const ExpPlan& pl, 
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    return launch_dependent(moe_expert_kernel<DOWN, MT>, sms, kExpThreads, pl.bytes, st, p, pl);
+    return launch_dependent(moe_expert_kernel<DOWN, MT>, sms < kMoeMaxGrid ? sms : kMoeMaxGrid, kExpThreads, pl.bytes, st, p, pl);
 }
 
 template <bool DOWN>

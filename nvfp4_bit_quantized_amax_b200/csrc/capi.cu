@@ -1141,7 +1141,7 @@ int adamw_overlap(const nvfp4_adamw_tensor* t, int count, const nvfp4_adamw_opts
     }
     *overlap = false;
     if (flat) return NVFP4_OK;
-    Span head[kKinds];
+    Span head[kKinds] = {};
     int next[kKinds] = {};
     bool ordered = true;
     auto advance = [&](int kind) {  // this kind's next buffer; past the last one an empty span at the end
@@ -1150,10 +1150,7 @@ int adamw_overlap(const nvfp4_adamw_tensor* t, int count, const nvfp4_adamw_opts
         while (head[kind].lo == head[kind].hi && head[kind].lo != UINTPTR_MAX);
         ordered &= head[kind].lo >= before;
     };
-    for (int kind = 0; kind < kinds; ++kind) {
-        head[kind].lo = 0;
-        advance(kind);
-    }
+    for (int kind = 0; kind < kinds; ++kind) advance(kind);
     SpanWalk walk;
     while (ordered) {
         int low = 0;

@@ -763,7 +763,11 @@ __global__ void __launch_bounds__(256) moe_sum_kernel(const MoeLayerParams p) {
 // ---------------------------------------------------------------- host side
 // Shared memory of a launch.  A pass takes as many tokens as an expert is likely to have
 // (its mean and two standard deviations), in tiles of 8 columns, while the rings keep 3
-// stages; very long rows leave room for fewer than 8 columns.
+// stages; for as many as it has usually (one deviation) 2 stages do, as a second pass costs
+// more.  3 and 2 there (us): 128 tokens, 32 experts of 2048 x 1024, top 4 105 and 94; 64 of 64
+// of 4096 x 2048, top 8 319 and 310; 128 of 64 of 1024 x 1024, top 8 98 and 94; 2 stages for the
+// likely number too: 64 tokens, 128 of 4096 x 2048, top 8 399 and 406.  Very long rows leave
+// room for fewer than 8 columns.
 static bool plan_expert(const MoeLayerParams& p, bool down, int smem_max, ExpPlan* pl) {
     const int parts = down ? kParts<true> : kParts<false>;
     const int row_bytes = 2 * (down ? p.F : p.K);
@@ -778,7 +782,8 @@ static bool plan_expert(const MoeLayerParams& p, bool down, int smem_max, ExpPla
         const int n = (room - columns * row_bytes - tiles * kExpWarps * 1024) / (kExpWarps * kStageBytes);
         return n > kMaxDepth ? kMaxDepth : n;
     };
-    while (nt > 1 && depth(nt * 8, nt) < 3) --nt;
+    const int usual = ((int)(mean + sqrt(mean)) + 1) * parts;
+    while (nt > 1 && depth(nt * 8, nt) < (nt * 8 - 8 < usual ? 2 : 3)) --nt;
     int columns = nt * 8;
     pl->cols = 8;
     while (columns > parts && depth(columns, nt) < 2) pl->cols = columns = columns / 2;

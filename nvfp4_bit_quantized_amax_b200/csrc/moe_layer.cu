@@ -215,15 +215,16 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 // 16 MMA).  All warps on one tile, for contiguous reads: above 560 (a join per tile).
 constexpr int kExpWarps = 16, kExpThreads = kExpWarps * 32;
 constexpr int kMaxTiles = 4;            // 8-column tiles of one pass
-// Share of the work.  With a dozen items or more a CTA, where experts have unlike numbers of
+// Share of the work.  From this many items a CTA on, where experts have unlike numbers of
 // tokens, an item counts as its passes over the weights plus its 8-column tiles; with fewer,
 // what counts is how many tiles a CTA's warps have to split at a time, and every item counts
 // alike.  Measured, alike and counted (us): 64 tokens, 128 experts of 4096 x 2048, top 8
-// (110 items a CTA) 539 and 390; 128 tokens, 64 of 1024 x 1024, top 8 (14 to 28) 96 and 83;
-// 128 tokens, 32 of 2048 x 1024, top 4 (14) 96 and 91; 32 tokens, 16 of 2048 x 1024, top 4
-// (7) 44 and 47; 128 tokens, 8 of 1024 x 512, top 2 (2) 38 and 50; against it 64 tokens, 8 of
-// 4096 x 2048, top 2 (7) 154 and 132.
-constexpr int kCountedItems = 12;
+// (110 items a CTA) 633 and 400; 128 tokens, 64 of 1024 x 1024, top 8 (14 to 28) 110 and 93;
+// 64 tokens, 8 of 4096 x 2048, top 2 (7) 178 and 143; 32 tokens, 16 of 2048 x 1024, top 4 (7)
+// 53.3 and 51.3; 48 tokens, 12 of 2048 x 1536, top 3 (5 to 8) 67.8 and 69.4; 128 tokens, 4 of
+// 4096 x 2048, top 2 (3.5) 215 and 294; 100 tokens, 10 of 1536 x 1536 without gate, top 2 (3) 66
+// and 75; 128 tokens, 8 of 1024 x 512, top 2 (2) 43 and 57.
+constexpr int kCountedItems = 6;
 constexpr int kMaxDepth = 5;            // stages of a warp's ring
 constexpr int kMoeMaxGrid = 256;        // CTAs of a projection
 constexpr int kScaleBytes = 2 * 40 * 4;  // two atoms' words of 32 rows, padded apart

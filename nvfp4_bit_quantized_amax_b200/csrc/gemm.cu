@@ -316,21 +316,23 @@ __device__ __forceinline__ void epilogue_tile(uint32_t lane_base, int64_t row0, 
             continue;
         }
         uint32_t r[32];
-        __syncwarp();  // as the fp32 stores of the columns before may have parted the lanes
         tmem_ld_32cols(lane_base + (uint32_t)(c * 32), r);
         tmem_wait_ld(r);
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(__uint_as_float(r[i]), alpha);
-        if (p.D_f32 && store && row < p.M) {
+        if (p.D_f32 && store) {
+            if (row < p.M) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int64_t col = col0 + c * 32 + 8 * g;
-                if (col >= p.N) break;
-                float4* d = reinterpret_cast<float4*>(p.D_f32 + row * p.N + col);
-                d[0] = make_float4(v[8 * g], v[8 * g + 1], v[8 * g + 2], v[8 * g + 3]);
-                d[1] = make_float4(v[8 * g + 4], v[8 * g + 5], v[8 * g + 6], v[8 * g + 7]);
+                for (int g = 0; g < 4; ++g) {
+                    const int64_t col = col0 + c * 32 + 8 * g;
+                    if (col >= p.N) break;
+                    float4* d = reinterpret_cast<float4*>(p.D_f32 + row * p.N + col);
+                    d[0] = make_float4(v[8 * g], v[8 * g + 1], v[8 * g + 2], v[8 * g + 3]);
+                    d[1] = make_float4(v[8 * g + 4], v[8 * g + 5], v[8 * g + 6], v[8 * g + 7]);
+                }
             }
+            __syncwarp();  // lanes together again for the next load of the accumulator
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -401,8 +403,9 @@ __device__ __forceinline__ void residual_fetch(const EpiCtx& x, int64_t col, int
 
 // The epilogue with bias, activation, residual and the copy of the value before the
 // activation (GemmParams): z = alpha acc + bias, D = act(z) + residual, each rounded
-// once from fp32.  The accumulator is released before the arithmetic (HOLD: all of the
-// warp's columns, as fp32, in registers), so that the next tile's MMAs run meanwhile.
+// once from fp32.  The accumulator is released before the arithmetic (HOLD: all 64 of the
+// warp's columns as fp32; with 736 threads a CTA's limit is 80 registers a thread, and ptxas
+// spills 300 bytes of them), so that the next tile's MMAs run meanwhile.
 // They share issue slots with this warp, so the arithmetic is in packed pairs.  All bf16
 // tensors move through the warp's staging buffer as boxes of CH columns, in the swizzle
 // of their tensor maps: 16-byte piece j of a row of 64 (32) bytes at j ^ ((row / 2) % 4)
@@ -530,7 +533,7 @@ __device__ __forceinline__ void epilogue_fused(uint32_t lane_base, int64_t row0,
         return;
     }
     if (HOLD) {
-        static_assert(!HOLD || CW == 64, "64 columns fit in registers");
+        static_assert(!HOLD || CW == 64, "a warp holds 64 columns");
         uint32_t r[64];
         tmem_ld_64cols(lane_base, r);
         tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(&r[0]));
@@ -1587,8 +1590,9 @@ cudaError_t launch_gemm(const GemmParams& p, int sm_count, cudaStream_t st) {
     return launch_gemm_cfg<256, 4, false>(p, sm_count, st);
 }
 
-// With the fused epilogue: sixteen epilogue warps on the pairs (64 columns each fit in
-// registers as fp32).
+// With the fused epilogue: sixteen epilogue warps on the pairs, each of which holds its 64
+// columns of a tile as fp32 (in part spilled).  Rows up to 128 take one-SM tiles of 128 x 256,
+// N / 256 CTAs that each walk all of K: with few columns most SMs idle.
 cudaError_t launch_gemm_epilogue(const GemmParams& p, int sm_count, cudaStream_t st) {
     if (sm_count >= 2 && p.M > 128) return launch_gemm_pair<5, false, 16, true>(p, sm_count, st);
     return launch_gemm_cfg<256, 4, false, true>(p, sm_count, st);

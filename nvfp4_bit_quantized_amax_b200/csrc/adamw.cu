@@ -14,10 +14,12 @@
 //
 // Bound by memory with 32-bit moments: 28 bytes an element (bf16 gradients and copies), 210M
 // elements in 860 us = 6.8 TB/s (a plain copy on the same machine moves 6.5).  With
-// 8-bit moments, 16 bytes, 101M elements in 351 us = 4.6 TB/s: 94 instructions an element, of
-// which the draws are 11, keep the issue slots 74% busy.  Packed arithmetic (78
-// instructions) alone gained nothing; with the next pass's loads ahead (64 registers) 2%,
-// while 32-bit moments became 12% slower.
+// 8-bit moments, 16 bytes, 101M elements in 354 us = 4.6 TB/s, short of both memory and issue
+// slots: 94 instructions an element (the draws are 11) keep those 74% busy, and the longest
+// stall is the wait for memory, one pass of loads being in flight.  Fewer instructions alone
+// (78, packed) gained nothing; those and the next pass's loads ahead 2%, which was not
+// worth the code.  Step and rate on the device cost two powers in fp64 per CTA before its
+// first load: 899 us against 863, and 373 against 356 with 8 bits.
 #include <cuda_bf16.h>
 #include <math.h>
 

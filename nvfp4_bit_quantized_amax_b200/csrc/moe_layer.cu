@@ -18,11 +18,13 @@
 // the second projection one of a token's two parts, side by side, so that one thread holds
 // both sums.
 //
-// Measured (a captured call, weights from memory): 64 experts of 2048 x 1024, top 4: 22 us
-// for 1 token, 55 us for 16 (146 MB of weights: 22 us at 6.5 TB/s); 128 experts of 4096 x
-// 2048, top 8, 64 tokens: 390 us for 1.8 GB (274 us), the projections at 5.1 and 4.8 TB/s.
-// What bounds it: few tokens, the chain of four launches; many, issue slots (56% busy with
-// four warps a scheduler, the latencies of decoding and MMA covered in part).
+// Measured (calls in a graph): 64 experts of 2048 x 1024, top 4: 22 us for 1 token, 54 us for
+// 16 (146 MB of weights: 22 us at 6.5 TB/s); 128 experts of 4096 x 2048, top 8, 64 tokens:
+// 404 us for 1.8 GB (274 us), the projections 233 and 137 us at 5.1 and 4.3 TB/s; 8 such
+// experts, top 2, 64 tokens: 142 us.  What bounds it: few tokens, the chain of four launches;
+// many, issue slots (56% busy with four warps a scheduler, the latencies of decoding and MMA
+// covered in part); more tokens an expert than shared memory holds rows, further passes over
+// its weights.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -173,6 +175,8 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
         const int j = threadIdx.x, e = chosen[j];
         double first = logit[chosen[0]];  // the largest chosen logit
         for (int i = 1; i < p.topk; ++i) first = fmax(first, logit[chosen[i]]);
+        // The weights go through fp32 exponentials of logits (softmax: of their differences)
+        // rounded to fp32: off by 2^-24 of the exponent and a few ulp, far below y's 2^-8.
         // Scores that are to be renormalized may share a factor: the softmax's total, and
         // e^first where the largest logistic is below a half, or all could vanish in fp32.
         const bool low = p.sigmoid && p.renormalize && first < 0.0;
@@ -207,7 +211,7 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 // borders of tiles, passes and segments: nothing is handed over between warps, so a
 // stage is refilled the moment it is in registers.  When fewer tiles than warps are left,
 // ks warps split a tile's columns and join their sums in order.
-//   First projection of 64 tokens, 128 experts of 4096 x 2048: 235 us; 378 while every CTA had
+//   First projection of 64 tokens, 128 experts of 4096 x 2048: 233 us; 378 while every CTA had
 // as many (expert, tile) pairs whatever the experts' tokens, against which: refilled after the
 // arithmetic: 397.  Stages filled by TMA from producer threads, four warps to a stage: 434
 // (264 with the arithmetic left out, but the way from use to refill is longer).  Weights

@@ -6,6 +6,7 @@ import torch
 from ffn_ref import U
 from gpu_util import DEV
 from nvfp4_bit_quantized_amax_b200 import capi
+from nvfp4_bit_quantized_amax_b200 import synthetic as syn
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +72,33 @@ def test_residual_with_fp32_output_alone(M, N, K):
     capi.nvfp4_gemm_epilogue(**kw, D_f32=d, bias=bias, act=capi.ACT_SILU, residual=res)
     capi.nvfp4_gemm_epilogue(**kw, D_f32=d2, D_bf16=d16, bias=bias, act=capi.ACT_SILU, residual=res)
     assert torch.equal(d, d2) and torch.equal(d.bfloat16(), d16)
+
+
+@pytest.mark.parametrize("block_mode,dgrad_rht", [(capi.BLOCK_16X16, 0), (capi.BLOCK_1X16, 0), (capi.BLOCK_1X16, 1)])
+def test_linear_fprop_in_place_and_its_options(block_mode, dgrad_rht):
+    """The residual in Y's place, the input in Y's place, both at once: as with buffers of their
+    own, and the workspace as nvfp4_linear_fprop_ex leaves it."""
+    M, K = 192, 256
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    X, res = (torch.randn(M, K, generator=gen, device=DEV).bfloat16() for _ in range(2))
+    W = (0.05 * torch.randn(K, K, generator=gen, device=DEV)).bfloat16()
+    bias = torch.randn(K, generator=gen, device=DEV)
+    signs = syn.rht_signs(2)
+
+    def call(x, y, **kw):
+        ws = torch.zeros(capi.linear_workspace_bytes(M, K, K), dtype=torch.uint8, device=DEV)
+        capi.nvfp4_linear_fprop_epilogue(x, W, y, signs, ws, act=capi.ACT_SILU, weight_block_mode=block_mode,
+                                         dgrad_rht=dgrad_rht, **kw)
+        assert capi.nvfp4_read_status(ws) == 0
+        return y, ws
+    want, ws = call(X, torch.empty_like(X), bias=bias, residual=res)
+    plain = torch.zeros_like(ws)
+    capi.nvfp4_linear_fprop_ex(X, W, torch.empty_like(X), signs, plain, weight_block_mode=block_mode, dgrad_rht=dgrad_rht)
+    assert torch.equal(ws, plain)
+    r = res.clone()
+    assert torch.equal(call(X, r, bias=bias, residual=r)[0], want)
+    x = X.clone()
+    assert torch.equal(call(x, x, bias=bias, residual=res)[0], want)
+    alone = call(X, torch.empty_like(X), residual=X)[0]
+    x = X.clone()
+    assert torch.equal(call(x, x, residual=x)[0], alone)

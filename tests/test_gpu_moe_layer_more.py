@@ -44,3 +44,21 @@ def test_router_with_parted_lanes(T, E, K):
     assert torch.equal(idx.long(), ridx)
     assert ((weight.double() - rw).abs() <= 2.0 ** -18 * rw + 1e-37).all()
     assert ((y.double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("T,E,topk,K,F", [
+    (128, 2, 2, 16384, 128),   # every token on both experts, four or two tokens a pass
+    (128, 2, 1, 128, 16384),
+    (127, 3, 3, 4096, 4096),
+    (128, 16, 16, 640, 640),   # every token on every expert
+    (65, 1024, 16, 256, 128),
+    (2, 2, 1, 16384, 16384),
+])
+@pytest.mark.parametrize("gated", [False, True])
+def test_many_passes_and_the_largest_sizes(T, E, topk, K, F, gated):
+    c = layer(T, E, topk, K, F, gated=gated, seed=T + K)
+    y, idx, _ = call(c)
+    ref, tol, ridx, _ = moe64(**c)
+    assert torch.equal(idx.long(), ridx)
+    assert ((y.double() - ref).abs() <= tol).all()
+    assert torch.equal(call(c)[0], y)

@@ -3,12 +3,12 @@
 //   dZ[m][n] = dY[m][n] act'(Z[m][n])      dbias[n] = sum over m of dZ[m][n]
 // (the residual's gradient is dY itself).  Memory-bound: 4 bytes read and 2 written per
 // element; 8192 x 20480 with GELU take 177 us in a replayed graph (5.7 TB/s), 184 to 188 called
-// with caches cleared.  A CTA takes 32 or 128 rows of 256
-// columns, 8 columns and every eighth row per thread, four rows' loads in flight at a time
-// (one row's: 246 us).  The column sums of the unrounded products, in fp32: the eight CTAs of
-// a cluster add theirs through distributed shared memory; with more rows than a cluster
-// has, its sums are a partial row, and a second kernel adds those up.  Every order is
-// fixed by M and N, so the sums do not depend on timing.
+// with caches cleared.  A CTA takes 32 or 128 rows of 256 columns, 8 columns and every eighth
+// row per thread, four rows' loads in flight at a time (one row's: 246 us).  The column sums
+// of the unrounded products, in fp32: the eight CTAs of a cluster add theirs through
+// distributed shared memory; with more rows than a cluster has, its sums are a partial row,
+// and a second kernel adds those up.  Every order is fixed by M and N, so the sums do not
+// depend on timing.
 #include <cuda_bf16.h>
 
 #include "activation.cuh"
@@ -21,9 +21,9 @@ constexpr int kBwdCluster = 8;
 // Rows per CTA: 32 while those CTAs are at most 1024, so that small problems spread and end
 // soon; else 128, which pays the cluster's barriers once per 16 rows of a thread.  1024 is
 // where the two meet as measured (registers allow four or five CTAs per SM, some 600 to 740 at
-// once, so the last of them run in a second wave).  GELU with sums, 32 and 128 rows (us): 250 x 264 3.4 and 7.5, 4096 x
-// 1024 7.9 and 11.5, 512 x 16384 (1024 CTAs) 12.3 and 16.7, 2048 x 4096 (1024) 12.2 and 12.1,
-// 4096 x 4096 23.4 and 20.0, 8192 x 20480 208 and 177.
+// once, so the last of them run in a second wave).  GELU with sums, 32 and 128 rows (us): 250 x
+// 264 3.4 and 7.5, 4096 x 1024 7.9 and 11.5, 512 x 16384 (1024 CTAs) 12.3 and 16.7, 2048 x 4096
+// (1024) 12.2 and 12.1, 4096 x 4096 23.4 and 20.0, 8192 x 20480 208 and 177.
 static inline int64_t bwd_rows(int64_t M, int64_t N) {
     return (N + kBwdCols - 1) / kBwdCols * ((M + 31) / 32) <= 1024 ? 32 : 128;
 }
